@@ -412,16 +412,28 @@ def _index(t, n, dtype, dev, what):
     return t.data_ptr()
 
 
-def _rows(t, n_rows, cols, stride, dev, what):
-    """fp16 rows `stride` elements apart on the current device: the last of n_rows must lie inside the tensor (or its
-    storage, where the rows are those of a wider tensor)."""
+def _rows(t, n_rows, cols, stride, dev, what, stated=False):
+    """fp16 rows `stride` elements apart on the current device: those of the tensor's first dimension, each contiguous, or
+    of a contiguous tensor cut into rows.  Where the caller states the stride, a flat buffer or a tensor of one row names
+    the start of the rows, and the last of them must lie inside its storage."""
     if t.dtype is not _torch.float16 or t.get_device() != dev:
         raise ValueError(f"{what}: an fp16 tensor on the current CUDA device")
-    if n_rows > 0 and not (t.dim() == 2 and t.stride(0) == stride and t.size(0) >= n_rows and t.size(1) >= cols
-                           and t.stride(1) == 1):
-        have = t.untyped_storage().nbytes() // 2 - t.storage_offset()
-        if t.stride(-1) != 1 or stride < cols or (n_rows - 1) * stride + cols > have:
-            raise ValueError(f"{what}: {n_rows} rows of {cols} values, {stride} apart, do not fit the tensor")
+    if n_rows <= 0 or (t.dim() == 2 and t.stride(0) == stride and t.size(0) >= n_rows and t.size(1) >= cols
+                       and t.stride(1) == 1):
+        return t.data_ptr()
+    inner = 1                       # values of a row, 0 when they do not lie together
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        inner = inner * size if step == inner or size == 1 else 0
+    if t.dim() >= 2 and t.size(0) >= n_rows and inner >= cols and (n_rows == 1 or t.stride(0) == stride):
+        return t.data_ptr()
+    need = (n_rows - 1) * stride + cols
+    if not stated:
+        fits = t.is_contiguous() and need <= t.numel() and (t.dim() == 1 or inner and stride % inner == 0)
+    else:
+        fits = (t.is_contiguous() or inner and (t.size(0) == 1 or t.dim() >= 2 and t.stride(0) == stride)) \
+            and need <= t.untyped_storage().nbytes() // 2 - t.storage_offset()
+    if not fits or stride < cols:
+        raise ValueError(f"{what}: {n_rows} rows of {cols} values, {stride} apart, are not those of the tensor")
     return t.data_ptr()
 
 
@@ -438,8 +450,8 @@ def fg_paged_append(cache: DevicePagedKVCache, k, v, row_stride: int, n_rows: in
     torch, dev, st = _ragged(stream)
     c, i32 = cache.c, torch.int32
     cache.check(dev)
-    _check(lib().fg_paged_append(cache.ref, _rows(k, n_rows, cache.h, row_stride, dev, "k"),
-                                 _rows(v, n_rows, cache.h, row_stride, dev, "v"), row_stride, n_rows,
+    _check(lib().fg_paged_append(cache.ref, _rows(k, n_rows, cache.h, row_stride, dev, "k", True),
+                                 _rows(v, n_rows, cache.h, row_stride, dev, "v", True), row_stride, n_rows,
                                  _index(row_start, c.B + 1, i32, dev, "row_start"), _index(pos0, c.B, i32, dev, "pos0"), st))
 
 
@@ -477,7 +489,7 @@ def fg_paged_attention(q, q_stride: int, cache: DevicePagedKVCache, lens, n_head
     if workspace is None:
         workspace = _made((fg_paged_attention_workspace_bytes(n_heads, cache.c.n_kv_heads, cache.c.head_dim),),
                           torch.uint8, dev, st)
-    _check(lib().fg_paged_attention(_rows(q, B, h, q_stride, dev, "q"), q_stride, cache.ref,
+    _check(lib().fg_paged_attention(_rows(q, B, h, q_stride, dev, "q", True), q_stride, cache.ref,
                                     _index(lens, B, torch.int32, dev, "lens"), n_heads, window, n_sink,
                                     _rows(out, B, h, h, dev, "out"), *_bytes(workspace, dev, "workspace"), st))
     return out
