@@ -11,7 +11,10 @@
 // and the order of that bin's few tokens, which are counted out.  Should the exact sums say that the prefix
 // ends in another bin, the search goes on with the approximate ones corrected by the difference.  A bin with
 // more than 512 tokens becomes the range of the next histogram; logits that are all equal are binned by their
-// ids.  The token is drawn by two levels of running sums in the order of the ids.
+// ids.  So do the tokens behind the last bin whose weights the approximation still tells apart (2^-14 of the range's
+// largest: one likely token and a top-p just above its probability): their histogram is relative to the largest of
+// them, so a row takes three histograms and eight passes at most over the distributions tried, however far down the cut lies.
+// The token is drawn by two levels of running sums in the order of the ids.
 //
 // What bounds it is instructions, not the 4 bytes of a logit: a row is read from HBM once and from L2 in
 // the later passes (maximum; total weight, for top-p alone; histogram, with a shared-memory atomic per token; kept
@@ -69,8 +72,8 @@ __device__ __forceinline__ u64 rank_of(float x, int id) {
 
 struct Shared {
   double table[kTable];       // 2^(i / 256)
-  uint32_t hist[kBins];       // counts of the bins, or approximate weights in steps of 2^-20 (a bin of 4096 tokens near
-                              // the maximum wraps: the exact sums then correct the search)
+  uint32_t hist[kBins];       // counts of the bins, or approximate weights in steps of 2^-20 of the largest considered (a
+                              // bin of 4096 tokens near it wraps: the exact sums then correct the search)
   u64 list[kList];            // rank values of this CTA's tokens in a cut's bin
   u64 merged[kList];          // those of the whole row (their weights then take the place of `list`)
   u64 cand[kCand];            // rank values of the tokens of this CTA that may be kept
@@ -300,11 +303,11 @@ __global__ void __launch_bounds__(kThreads, (ctas == 1 ? 2 : 1))
     if (by == kLinear) return int(fminf((x_hi - v) * scale, float(kBins - 1)));
     return by == kKeys ? int((key_of(x_hi) - key_of(v)) >> shift) : id >> shift;
   };
-  // the weight in fp32, in steps of 2^-20: near enough to name a bin
-  const float c32 = float(weight.c);
+  // the weight in fp32, in steps of 2^-20 of that of x_hi: near enough to name a bin
+  const float c32 = fminf(float(weight.c), 3.402823466e38f);  // finite: x_hi itself has 2^20 at any temperature
   auto rough = [&](float v) {
     float w;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(v - weight.m, c32, 20.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(v - x_hi, c32, 20.f)));
     return weight.m == INFINITY ? uint32_t(v == INFINITY) << 20 : __float2uint_rn(w);
   };
   // f(logit, id) for the tokens of this CTA's list or ids.  Every lane of a warp makes the same calls.
@@ -422,17 +425,19 @@ __global__ void __launch_bounds__(kThreads, (ctas == 1 ? 2 : 1))
     int list_bin = -1;  // the last bin whose tokens the list holds, where it was made here
     bool may_list = !listed && by == kLinear;
     for (;;) {
-      // before this thread's bins, in the units of what is needed: tokens, or weights in steps of 2^-20 (from 2^-44)
-      const u64 pre = before_bins() + (by_n ? above_n : above_w >> 24);
+      // before this thread's bins: tokens of the row, or weights of those considered in the histogram's steps
+      const u64 pre = before_bins() + (by_n ? above_n : 0);
+      const double step = by_n ? 1.0 : double(weight(x_hi)) * 9.5367431640625e-07;  // 2^-20
       int first = 0, last = kBins - 1;                                            // the bin lies between these
-      int64_t fix = 0;                                                            // of the approximate weights
+      u64 done = above_w;                                                         // weight of what comes before `first`
+      double fix = 0.0;                                                           // of the approximate weights
       u64 n_before = 0, a = 0, in = 0, n_in = 0;
       int bin = -1;
+      bool behind = false;  // the cut lies behind the bins whose approximate weights say anything
       for (;;) {
         // the first bin that reaches what is needed, else the last with anything in it
-        bin = first_bin(pre, first, last, [&](u64 e) {
-          return by_n ? e >= need_n : double(int64_t(e) + fix) >= need_w * 5.9604644775390625e-08;  // 2^-24
-        });
+        const double left = by_n ? 0.0 : (need_w - double(above_w) - fix) / step;
+        bin = first_bin(pre, first, last, [&](u64 e) { return by_n ? e >= need_n : double(e) >= left; });
         if (bin == kBins) {
           if (by_n) return 0;
           if (tid == 0) sh.bin = -1;
@@ -445,7 +450,10 @@ __global__ void __launch_bounds__(kThreads, (ctas == 1 ? 2 : 1))
           sync();
           bin = -1;
           of_all(&sh.bin, [&](int, int v) { bin = max(bin, v); });
-          if (bin < 0) bin = first;  // nothing with an approximate weight: bin by bin
+          if (bin < 0) {
+            behind = true;
+            break;
+          }
         }
         if (may_list) {
           // the tokens up to the bin (and the next one, for what is approximate), from their weights
@@ -504,18 +512,28 @@ __global__ void __launch_bounds__(kThreads, (ctas == 1 ? 2 : 1))
         const bool back = double(a) >= need_w && bin_at(weight.m, 0) != bin && first < bin;
         const bool on = double(a + in) < need_w && bin < last;
         if (!back && !on) break;
-        (back ? last : first) = back ? bin - 1 : bin + 1;
-        fix = int64_t(a >> 24) - int64_t(e);
+        if (back) {
+          last = bin - 1;
+        } else {
+          first = bin + 1;
+          done = a + in;
+          behind = double(in) < 64.0 * step * double(n_in);  // what follows weighs less than 64 steps a token
+          if (behind) break;
+        }
+        fix = double(a - above_w) - double(e) * step;
         sync();  // the lists' lengths have been read
       }
-      above_w = a;
+      if (!behind) first = last = bin;
+      if (list_bin >= 0 && last > list_bin) listed = false;
+      above_w = behind ? done : a;
       above_n = n_before;
       list_bin = -1;
-      if (n_in <= kList) break;
-      // too many for the list: the bin becomes the range of the next histogram
+      if (!behind && n_in <= kList) break;
+      // too many for the list, or too far down: the bin, or those that are left, become the range of the next histogram
       u64 mx = 0, mn = ~u64(0);
       each([&](float v, int id) {
-        if (bin_at(v, id) == bin) {
+        const int at = bin_at(v, id);
+        if (at >= first && at <= last) {
           const u64 r = rank_of(v, id);
           mx = max(mx, r);
           mn = min(mn, r);
