@@ -21,8 +21,9 @@
 //   score_t = sum_n s_tn D_tn + mn_tn (sum_{d in n} q_d),
 //   out_d = sum_t (p_t s_tn) c_td + sum_t p_t mn_tn,   n the group of d,
 // with q scaled by a power of two so that its largest value is near 2^12, and the weights p_t s_tn
-// rounded to fp16 relative to a power of two near the largest s of the group so far (2^-11 each;
-// both scalings are exact).  What a weight's rounding took off is added back in fp32 with the mean code 7.5
+// rounded to fp16 relative to a power of two near the largest s of the group that the warp has seen (2^-11 of
+// each weight down to 2^-14 of that reference, 2^-25 of the reference below; both scalings are exact).  What a
+// weight's rounding took off is added back in fp32 with the mean code 7.5
 // (a part of the sum over mn), so that the rounding counts against c - 7.5, not against c: on the larger cases
 // the error drops from 2.7 to 1.5 times that of the output's own rounding.  The softmax is fp32 with exp2; the running maximum of a row is raised only
 // when a score passes it by more than 2^8, so the usual tile needs one vote.
@@ -51,6 +52,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTP = 64;  // positions per tile: 4 blocks of 16
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kUnset = 536870912.f;  // 2^29, before any value scale was seen: the smallest one in fp16, 2^-24, passes 16 with it
 constexpr float kMid = 7.5f;  // the mean code, which what the rounding of a weight takes off is given back with
 
 // CTAs per SM, a matter of room alone: registers allow 2 with 16 query rows, 3 below; shared memory 3 up to tiles of 9216 bytes
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, G, RW, NT>::CTAS))
         for (int i = 0; i < HD / 16; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < NG; ++n) inv[n] = 1.f, mid[n] = kMid;
+      for (int n = 0; n < NG; ++n) inv[n] = kUnset, mid[n] = kMid / kUnset;
     }
 
 #pragma unroll
@@ -487,8 +489,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, G, RW, NT>::CTAS))
 
       // ---- raise the maximum of a row, or the reference of a group's value scales, where they fell behind
       float top[NT][RE], smax[NG];
-      const bool first = b0 == 0 && (flags & kFirst);
-      bool raise = first;
+      bool raise = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, G, RW, NT>::CTAS))
         for (int n = 0; n < NG; ++n) {
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) smax[n] = fmaxf(smax[n], __shfl_xor_sync(0xffffffffu, smax[n], o));
-          if ((first || smax[n] * inv[n] > 16.f) && smax[n] > 0.f && smax[n] < INFINITY) {
+          if (smax[n] * inv[n] > 16.f && smax[n] < INFINITY) {  // the first scale above 0 always
             const float to = __uint_as_float((253u << 23) - (__float_as_uint(smax[n]) & 0x7f800000u));  // smax to [0.5, 1)
             const float r = to / inv[n];  // a power of two
             inv[n] = to;

@@ -362,3 +362,31 @@ def test_append_of_small_and_large_ranges_is_exact(fg, scale):
     fg.fg_paged_append(dev, to_dev(k), to_dev(v), nkv * hd, n, i32([0]), row_start=i32([0, n]))
     cpu.append(k, v, np.array([0, n]), [0])
     same_cache(dev, cpu)
+
+
+@pytest.mark.parametrize("vscale", [1e-4, 1e-5])
+@pytest.mark.parametrize("rep", [1, 2, 4, 8, 16])
+def test_paged_attention_small_values_wherever_the_window_starts(fg, rep, vscale):
+    """The fp16 weights are relative to the value scales that are seen, also where the first positions of the first tile are
+    not: before the window, in a page that is not there, or with values that are all equal (scale 0)."""
+    nkv, hd, group, page = 2, 64, 32, 16
+    lens = [30, 17, 64, 100, 127, 128, 50]
+    r, dev, cpu = filled(fg, rep, lens, nkv, hd, group, page, vscale=vscale)
+    nh = nkv * rep
+    q = rows(r, len(lens), nh * hd)
+    for window in (1, 2, 9, 14, 33, 47, 60):
+        out = fg.fg_paged_attention(to_dev(q), nh * hd, dev, i32(lens), nh, window=window)
+        check(to_np(out), q, cpu, lens, nh, window)
+    table = cpu.table.copy()
+    for i in range(4):                      # the first pages of a sequence are not there
+        table[3 + i % 3, i] = -1
+    dev.page_table.copy_(i32(table))
+    cpu.table = table
+    out = fg.fg_paged_attention(to_dev(q), nh * hd, dev, i32(lens), nh)
+    check(to_np(out), q, cpu, lens, nh)
+    for b in range(len(lens)):              # a page of equal values, then the others
+        p = next((int(p) for p in table[b] if p >= 0), None)
+        dev.v_params[p, :, :, :, 1] = 0
+    cpu.params = [to_np(dev.k_params), to_np(dev.v_params)]
+    out = fg.fg_paged_attention(to_dev(q), nh * hd, dev, i32(lens), nh)
+    check(to_np(out), q, cpu, lens, nh)
