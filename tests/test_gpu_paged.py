@@ -390,3 +390,24 @@ def test_paged_attention_small_values_wherever_the_window_starts(fg, rep, vscale
     cpu.params = [to_np(dev.k_params), to_np(dev.v_params)]
     out = fg.fg_paged_attention(to_dev(q), nh * hd, dev, i32(lens), nh)
     check(to_np(out), q, cpu, lens, nh)
+
+
+def test_paged_attention_heads_past_2_32_bytes_of_a_page(fg):
+    """More key/value heads than 4 GiB of a page's codes hold: the last ones are read from where append put them."""
+    import torch
+    nkv, hd, g, page, n = (1 << 16) + 4, 128, 128, 1024, 3
+    h = nkv * hd
+    dev = fg.DevicePagedKVCache(i32([[0]]), nkv, hd, 1, page, g)
+    r = np.random.default_rng(41)
+    k, v, q = rows(r, n, h), rows(r, n, h), rows(r, 1, h)
+    fg.fg_paged_append(dev, to_dev(k), to_dev(v), h, n, i32([0]), row_start=i32([0, n]))
+    heads = [0, 1, 3, nkv - 5, nkv - 4, nkv - 1]
+    pick = lambda x: x.reshape(len(x), nkv, hd)[:, heads].reshape(len(x), -1)   # noqa: E731
+    small = ref.Paged(np.array([[0]]), len(heads), hd, 1, page, g)
+    small.append(pick(k), pick(v), [0, n], [0])
+    for i, codes in enumerate((dev.k_codes, dev.v_codes)):
+        assert np.array_equal(to_np(codes[0, heads, :n]), small.codes[i][0, :, :n])
+    out = fg.fg_paged_attention(to_dev(q), h, dev, i32([n]), nkv)
+    check(pick(to_np(out)), pick(q), small, [n], len(heads))
+    del dev
+    torch.cuda.empty_cache()
