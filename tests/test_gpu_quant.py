@@ -194,3 +194,68 @@ def test_kv_append_prompt_size_sampled(fg):
         assert np.array_equal(to_np(cache.k_params[b, :, sl]).view(np.uint16), ref.k_params[0, :, sl].view(np.uint16))
         assert np.array_equal(to_np(cache.v_params[b, :, sl]).view(np.uint16), ref.v_params[0, :, sl].view(np.uint16))
         assert not to_np(cache.k_codes[b, :, :off]).any() and not to_np(cache.v_codes[b, :, off + T:]).any()
+
+
+def _small_groups():
+    """Every value i 2^-24 of groups with every subnormal scale s = j 2^-24 (and those just above), from groups of 64 values
+    with minimum 0 and a range of 15 j - 7 .. 15 j + 7 of the steps: (values in steps [groups, 64], j)."""
+    rows, js = [], []
+    for j in list(range(1, 1024)) + [1030, 1100, 2000]:
+        for top in ([15 * j - 7, 15 * j, 15 * j + 7] if j < 40 else [15 * j + 7 - j % 15]):
+            v = np.arange(1, top)
+            v = np.concatenate([v, np.full(-len(v) % 62, top)]).reshape(-1, 62)
+            rows.append(np.concatenate([np.zeros((len(v), 1), np.int64), v, np.full((len(v), 1), top)], 1))
+            js += [j] * len(v)
+    return np.concatenate(rows), np.array(js)
+
+
+@pytest.mark.parametrize("shift", [False, True])
+def test_pack_every_subnormal_scale_is_exact(fg, shift):
+    """Codes of the definition in whole numbers: i / j to even, held at 15 (scales of a few steps reach 22)."""
+    i, j = _small_groups()
+    if shift:       # minima below zero; what fp16 cannot hold in steps of 2^-24 is left out
+        ok = j < 250
+        i, j = i[ok], j[ok]
+        x = ((i - i.max(1, keepdims=True) // 2) * 2.0 ** -24).astype(np.float16)
+    else:
+        ok = i.max(1) < 2048 * 2
+        i, j = i[ok], j[ok]
+        i = np.where(i >= 2048, i & ~1, i)           # fp16's own steps above 2^-13
+        x = (i * 2.0 ** -24).astype(np.float16)
+    steps = x.astype(np.float64) * 2.0 ** 24
+    steps -= steps.min(1, keepdims=True)
+    s = np.rint(steps.max(1) / 15)                   # the scale in steps: fp16 subnormals are whole numbers of them
+    assert np.all(s < 1024) and np.all(steps == np.rint(steps))
+    want = np.minimum(np.where(s[:, None] == 0, 0, np.rint(steps / np.maximum(s, 1)[:, None])), 15).astype(np.uint8)
+    codes, params = fg.fg_quantize_pack(to_dev(x), 64, 1)
+    got = to_np(codes)
+    assert np.array_equal(to_np(params)[:, 0, 1].astype(np.float64) * 2.0 ** 24, s)
+    assert np.array_equal(got & 15, want[:, 0::2]) and np.array_equal(got >> 4, want[:, 1::2])
+
+
+@pytest.mark.parametrize("scale", [0.01, 3e-3, 1e-4, 1e-6])
+def test_pack_around_the_smallest_normal_scale(fg, scale):
+    _check_pack(fg, fg_synth.tensor(29, 3, (61, 1536), "normal", scale), 64, 1)
+
+
+def test_pack_of_small_values_takes_no_longer_than_a_few_instructions_more(fg):
+    """Subnormal scales are quantized without divisions: 0.98 and 1.32 of the time of N(0, 1); 3.0 by division."""
+    import torch
+    x = torch.randn((32768, 4096), device="cuda")
+
+    def time(x):
+        ts = []
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            a.record()
+            fg.fg_quantize_pack(x, 64, 1)
+            b.record()
+            torch.cuda.synchronize()
+            ts.append(a.elapsed_time(b))
+        return min(ts[2:])
+    usual = time(x.half())
+    for scale in (1e-4, 1e-6):
+        t = time((x * scale).half())
+        print(f"scale {scale}: {t / usual:.2f} of {usual * 1e3:.0f} us")
+        assert t <= 2 * usual
