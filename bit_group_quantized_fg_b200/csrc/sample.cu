@@ -451,8 +451,9 @@ __global__ void __launch_bounds__(kThreads, (ctas == 1 ? 2 : 1))
           bin = -1;
           of_all(&sh.bin, [&](int, int v) { bin = max(bin, v); });
           if (bin < 0) {
-            behind = true;
-            break;
+            behind = first > 0;  // (the bin of x_hi is among those done: the next range is a smaller one)
+            if (behind) break;
+            bin = first;  // all sums wrapped to 0: the exact ones of the first bin say how to go on
           }
         }
         if (may_list) {
