@@ -411,3 +411,42 @@ def test_paged_attention_heads_past_2_32_bytes_of_a_page(fg):
     check(pick(to_np(out)), pick(q), small, [n], len(heads))
     del dev
     torch.cuda.empty_cache()
+
+
+def middle_tol(cpu, b, n, j, q):
+    """Budget of head j's output when what a weight's rounding took off is given back with the mean code: the rounding
+    2^-11 p s is multiplied by c - 7.5 in place of c (the other terms as in attend_tol)."""
+    k, v, rise, there = cpu.gather(b, n)
+    pages, t = cpu.table[b, np.arange(n) // cpu.page], np.arange(n) % cpu.page
+    s = np.repeat(cpu.params[1][pages, j, t, :, 1].astype(np.float64), cpu.group, axis=-1)
+    out, (mass, size, _, vmax) = ref.attend(q, k[j], v[j], there, rise[j])
+    e = np.exp(k[j] @ q / np.sqrt(cpu.hd) - (k[j] @ q / np.sqrt(cpu.hd)).max())
+    off = (e / e.sum()) @ np.abs(rise[j] - 7.5 * s)
+    fp32 = 2 * (16 * 2.0 ** -23 * size + 2.0 ** -22) + 128 * 2.0 ** -23
+    return out, 2.0 ** -11 * np.abs(out) + 2.0 ** -25 + 2.0 ** -11 * off + fp32 * mass + n * 2.0 ** -25 * vmax
+
+
+@pytest.mark.parametrize("hd,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("rep", [1, 2, 4, 8, 13])
+def test_paged_attention_gives_back_what_the_weights_lost(fg, hd, group, rep):
+    """Values whose codes are 7 and 8 but for the two ends of a group, and whose outputs are small: their error is that of
+    half a code, not of seven and a half."""
+    nkv, page, lens = 3, 16, [2, 3, 5, 8, 13, 40]
+    r = np.random.default_rng(hd + group + rep)
+    dev, cpu = pair(fg, r, lens, nkv, hd, group, page)
+    start, n = np.concatenate([[0], np.cumsum(lens)]), int(sum(lens))
+    v = r.choice([-0.5, 0.5], (n, nkv * hd // group, group)) * r.uniform(0.2, 1.0, (n, nkv * hd // group, 1))
+    v[:, :, 0], v[:, :, 1] = -7.5 * np.abs(v[:, :, 2]) * 2, 7.5 * np.abs(v[:, :, 2]) * 2
+    k, v = rows(r, n, nkv * hd), v.reshape(n, -1).astype(np.float16)
+    fg.fg_paged_append(dev, to_dev(k), to_dev(v), nkv * hd, n, i32([0] * len(lens)), row_start=i32(start))
+    cpu.codes, cpu.params = [to_np(dev.k_codes), to_np(dev.v_codes)], [to_np(dev.k_params), to_np(dev.v_params)]
+    q = rows(r, len(lens), nkv * rep * hd)
+    out = to_np(fg.fg_paged_attention(to_dev(q), nkv * rep * hd, dev, i32(lens), nkv * rep)).astype(np.float64)
+    worst = 0.0
+    for b, m in enumerate(lens):
+        for j in range(nkv * rep):
+            x = q[b, j * hd:(j + 1) * hd].astype(np.float64)
+            want, tol = middle_tol(cpu, b, m, j // rep, x)
+            worst = max(worst, float(np.max(np.abs(out[b, j * hd:(j + 1) * hd] - want) / tol)))
+    print("worst / tolerance", worst)
+    assert worst <= 1.0
