@@ -34,12 +34,13 @@
 // product of block i takes the weights in the columns of copy i and zeros elsewhere.  The copies
 // are added up at the end of a context.
 //
-// Measured: 256 sequences of 543 positions, 56 heads of 128 (784 MB): 174 us, 4.5 TB/s, 69 % of a
+// Measured: 256 sequences of 543 positions, 56 heads of 128 (784 MB): 165 to 176 us on different GPUs, 4.5 TB/s, 69 % of a
 // copy's rate; 8 sequences of 32k, 32 query heads on 8 (194 MB): 53 us; 48 sequences that see 4096
-// positions, 32 on 4 (117 MB): 50 us; 1 sequence of 700, 12 heads of 64: 10 us, two launches.  What
-// bounds it is no longer HBM but the integer pipe (59 % busy in the first case, with 900 instructions
-// per tile of 64 positions): taking the codes apart.  Shared by a group of query heads, a tile costs
-// more of the softmax and as much of that, so the rate falls with the heads per key/value head.
+// positions, 32 on 4 (117 MB): 50 us; 1 sequence of 700, 12 heads of 64: 10 us, two launches.  No unit
+// is saturated.  In the first case (930 instructions per tile of 64 positions) DRAM is 72 % busy, the integer
+// pipe, which takes the codes apart, 58 %, the issue slots 52 %, with 10 warps per SM to hide the rest; in the
+// third (1790 instructions per tile: a softmax pass per 16 positions, four groups per head) the issue slots 48 %, the
+// integer pipe 33 %, with 7 warps per SM.
 #include <algorithm>
 
 #include "paged_common.cuh"

@@ -22,7 +22,7 @@
 //            any key of, which is raised (and O rescaled) only when the weights of a tile add up to more than 2^13: until then
 //            every P fits fp16 and the fp32 sums with the same relative precision as against the true
 //            maximum, and no maximum has to be taken.
-// What bounds it: the tensor cores and the exponentials in turn (with the exponentials left out 2 x 8191
+// What bounds it: the tensor cores and the exponentials in turn (each 53 % busy; with the exponentials left out 2 x 8191
 // rows still took 480 us of 560), where keys are many; HBM and the start of items where they are few.
 // Measured: 2 sequences of 8191, window 2048, 32 heads on 8 (498 GFLOP): 525 us cold, 608 us repeated
 // under the power limit; 64 x up to 512, 32 heads of 128 (802 MB): 238 us, 275 us repeated; 4 x 32, 12 heads

@@ -119,7 +119,7 @@ __device__ __forceinline__ GroupQ quantize_chunk16(uint4 a, uint4 b) {
   const uint64_t MN2 = f2_pack(mn, mn), RCP2 = f2_pack(rcp, rcp), MAG2 = f2_pack(kMagic, kMagic);
   const uint64_t C256 = f2_pack(256.f, 256.f);
   // The integers q stand in T - magic; four of them are put together by exact fp32 sums, magic + q0 + 256 q2 + 16 (q1
-  // + 256 q3) < 2^24, whose low half then holds the four codes (1 GiB, group 64: 272 -> 259 us against a minimum, shifts
+  // + 256 q3) < 2^24, whose low half then holds the four codes (1 GiB, group 64: 273 -> 262 us against a minimum, shifts
   // and ORs per code).  That no q passes 15 needs a scale that is not too small: s is (mx - mn) / 15 to
   // 2^-25 at most where it is subnormal, so r <= 15 (1 + 2^-5) < 15.5 from s = 2^-20 on; smaller and infinite scales and
   // NaNs take the paths out of line.

@@ -13,7 +13,8 @@
 // more than 512 tokens becomes the range of the next histogram; logits that are all equal are binned by their
 // ids.  So do the tokens behind the last bin whose weights the approximation still tells apart (2^-14 of the range's
 // largest: one likely token and a top-p just above its probability): their histogram is relative to the largest of
-// them, so a row takes three histograms and eight passes at most over the distributions tried, however far down the cut lies.
+// them, so a row takes four histograms and ten passes at most over the distributions tried (two passes usually), however far
+// down the cut lies.
 // The token is drawn by two levels of running sums in the order of the ids.
 //
 // What bounds it is instructions, not the 4 bytes of a logit: a row is read from HBM once and from L2 in
@@ -28,11 +29,11 @@
 // Few rows are shared by a cluster of up to 8 CTAs, each with a range of the ids and a share of the bins, which
 // exchange maxima, bins, sums and lists through distributed shared memory and all come to the same results.
 //
-// 256 rows of 50272 logits (51 MB; copying them takes 8 us): 37 us with top-k 40, 53 us with top-k 40 and
-// top-p 0.9 (80 us without the list), 45 us without a filter, 82 / 102 us with top-p 0.5 / 0.9 of a flat
-// distribution, 19 us for the largest logit; all settings mixed 108 us.  3 rows of 128001 on clusters of 8 CTAs: 29, 45,
-// 18, 53 / 57 and 10 us.
-//
+// Logits of N(0, 1), calls back to back over 300 MB of them.  256 rows of 50272 (51 MB; copying them takes 8 us): 32 us
+// with top-k 40, 39 us with top-k 40 and top-p 0.9, 39 us without a filter, 117 / 139 / 167 us with top-p 0.5 / 0.9 / 0.999,
+// 14 us for the largest logit.  3 rows of 128001 on clusters of 8 CTAs: 25, 37, 14, 52 / 55 / 55 and 9 us.  With settings
+// mixed by row a batch takes as long as its slowest kind of row (all 256 CTAs are resident at once, a row each): 105 to
+// 132 us and 31 to 37 us, by which settings were drawn and by their logits.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -750,9 +751,10 @@ int sample_impl(const float* logits, int64_t ld, int B, int V, const float* temp
   FG_TRY(check_sample(logits, ld, B, V, temperature, top_k, top_p, min_p, u, tokens, logprob));
   if (B == 0) return FG_OK;
   ProfScope ps(PROF_OTHER, s, 0.0, double(B) * V * 4.0);
-  // CTAs per row: as many as find an SM each, with at least 7168 ids.  24 rows of 50272, top-k 40 and top-p 0.9: 37 us
-  // on 4 CTAs, 78 us on 8, which take two rounds; one row: 37 us on 4, 43 us on 8.  3 rows of 128001: 52 us on 8, 90 us
-  // on 1.  256 rows of 50272: 108 us on 1 (two CTAs share an SM), 136 us on 2.
+  // CTAs per row: as many as find an SM each, with at least 7168 ids.  Top-p 0.9 (top-k 40 and top-p 0.9 behind the comma),
+  // N(0, 1): 24 rows of 50272 45, 31 us on 4 CTAs, 92, 71 on 8, which take two rounds, 65, 33 on 2, 100, 29 on 1; one row 44, 29
+  // on 4, 46, 35 on 8.  3 rows of 128001: 55, 37 us on 8, 75, 33 on 4, 225, 38 on 1.  256 rows of 50272: 139, 39 us on 1 (two
+  // CTAs share an SM), 248, 127 on 2.
   int ctas = 1;
   while (ctas < 8 && int64_t(B) * ctas * 2 <= num_sms() && V >= ctas * 14336) ctas *= 2;
   if (int64_t(B) * ctas > 0x7fffffff) return fail(FG_ERR_SHAPE, "too many rows");

@@ -241,8 +241,8 @@ int fg_lm_head_argmax(const void* x, int B, int hidden, const void* E, int vocab
  *
  * Index arrays are 4-byte aligned device int32.  Their values cannot be checked on the host;
  * the kernels check them: every call states what it does with an index out of range, and none
- * reads or writes outside the buffers it is given.  A call without rows (n_rows, n_q or B of the
- * sampler 0) does nothing and may name no buffers.
+ * reads or writes outside the buffers it is given.  A call without rows (n_rows, n_q or fg_sample's
+ * B 0) does nothing and may name no buffers.
  * ---------------------------------------------------------------------------------- */
 
 /* A paged 4-bit KV cache of one layer.  Position t of sequence b lies in page
@@ -334,7 +334,7 @@ int fg_sample(const float* logits, int64_t ld, int B, int vocab, const float* te
               const float* top_p, const float* min_p, const float* u, int32_t* tokens, float* logprob, void* stream);
 
 /* The tied LM head of fg_lm_head_argmax followed by fg_sample instead of the arg max; same
- * conditions (the head's product needs vocab % 8 == 0, FG_ERR_SHAPE), workspace >=
+ * conditions (B >= 1 and, for the head's product, vocab % 8 == 0: FG_ERR_SHAPE), workspace >=
  * fg_lm_head_workspace_bytes when `logits` is NULL. */
 int fg_lm_head_sample(const void* x, int B, int hidden, const void* E, int vocab, float* logits,
                       const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
