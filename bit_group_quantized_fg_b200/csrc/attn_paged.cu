@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, G, RW, NT>::CTAS))
     __syncwarp();  // the barrier expects its bytes before the first of them can land
     if (ok) {
       const int in_page = (i_pos + piece * psize) & ((1 << c.page_shift) - 1);
-      const uint8_t* src = src0 + i_page * page_bytes + (int64_t(NT == 1 ? i_h : i_h / n_rt) * head_bytes + in_page * rb);
+      const uint8_t* src = src0 + i_page * page_bytes + (uint64_t(uint32_t(NT == 1 ? i_h : i_h / n_rt)) * head_bytes + uint32_t(in_page * rb));
       bulk_load(dst0 + sl * C::SLOT, src, bytes, &bars[warp][sl]);
     }
     // on to the next tile, whose page is looked up here, an iteration before its copy
